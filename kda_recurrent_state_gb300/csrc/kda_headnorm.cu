@@ -5,7 +5,7 @@
 //   y = n with its first `rot` entries turned in pairs (a, b) by the angle of (m, pair):
 //       (a cos - b sin, a sin + b cos), pairs (i, i + rot/2) or (2i, 2i + 1).
 // Backwards, with g = dy turned back:  dw = sum g r x,   h = g w,
-//   dx = r h - x r^3 s <h, x>,   s = 1/d (RMS), 1 (L2), 0 (none).
+//   dx = r h - x r^3 s <h, x>,   s = 1/d (RMS), 1 (L2);   dx = h (none: x has no part in it).
 //
 // Bound by HBM: each head is read once and written once.  A head is held by a power of two of
 // lanes, 8 channels each (16 bytes of bf16, 32 of fp32), so its sums are shuffles and the half
@@ -26,13 +26,13 @@ constexpr int kThreads = 128;
 constexpr int kMaxHead = 256;
 constexpr int kBwdBlocks = 152 * 4;
 
-// 1 / norm, and the factor s of the gradient.
+// 1 / norm, and the factor s of a norm's gradient.
 __device__ __forceinline__ float inv_norm(const HeadProblem& p, float ss) {
     if (p.norm == KDA_NORM_NONE) return 1.f;
     return rsqrtf((p.norm == KDA_NORM_RMS ? ss / (float)p.d : ss) + p.eps);
 }
 __device__ __forceinline__ float grad_share(const HeadProblem& p) {
-    return p.norm == KDA_NORM_RMS ? 1.f / (float)p.d : p.norm == KDA_NORM_L2 ? 1.f : 0.f;
+    return p.norm == KDA_NORM_RMS ? 1.f / (float)p.d : 1.f;
 }
 
 // Row of the angle tables for a token, or -1 (not turned): no rotation, or a position outside
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) head_norm_bwd_kernel(HeadProblem p) 
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dw[i] = fmaf(g[i], v[i] * inv, dw[i]);
-                v[i] = fmaf(gw[i], inv, -v[i] * back);
+                v[i] = p.norm == KDA_NORM_NONE ? gw[i] : fmaf(gw[i], inv, -v[i] * back);
             }
             if (mine && k < n) st_vec<8>(dx + k * p.d, v);
         }
@@ -410,7 +410,8 @@ __global__ void __launch_bounds__(kThreads) head_norm_any_kernel(HeadProblem p) 
                 if (e < p.d) {
                     float f[1] = {fmaf(g[i], inv, -v[i] * back)};
                     // one channel: h and x are parallel, and 1 - x^2 r^2 = eps r^2 takes the place of the difference
-                    if (p.d == 1 && p.norm != KDA_NORM_NONE) f[0] = g[i] * inv * (p.eps * inv * inv);
+                    if (p.d == 1) f[0] = g[i] * inv * (p.eps * inv * inv);
+                    if (p.norm == KDA_NORM_NONE) f[0] = g[i];
                     st_vec<1>(static_cast<To*>(p.y[which]) + o + e, f);
                 }
             }
