@@ -73,15 +73,18 @@ __device__ __forceinline__ void ld_floats(const float* src, bool vec, float (&f)
 }
 
 // The angles of a lane's 8 channels: for halves c[i], s[i] of channel i (s negative in the first
-// half, so y = x c + partner s); for neighbours c[j], s[j], j < 4, of its pairs.
+// half, so y = x c + partner s); for neighbours c[j], s[j], j < 4, of its pairs.  The first `live` channels
+// are turned; the rest are left as they are, not turned by 0: an infinity or NaN times 0 would spread.
 struct Angles {
     float c[8], s[8];
+    int live;
 };
 template <bool kMixed>
 __device__ __forceinline__ void load_angles(const HeadProblem& p, int64_t row, int e0, Angles& a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) { a.c[i] = 1.f; a.s[i] = 0.f; }
-    if (row < 0 || e0 >= p.rot) return;
+    a.live = row < 0 ? 0 : p.rot - e0;
+    if (a.live <= 0) return;
     const int half = p.rot / 2;
     const float* c = p.cos + row * half;
     const float* s = p.sin + row * half;
@@ -129,21 +132,23 @@ __device__ __forceinline__ void turn(const HeadProblem& p, const Angles& a, floa
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int e = e0 + i, o = e < half ? e + half : e < p.rot ? e - half : e;
-            v[i] = fmaf(v[i], a.c[i], ex[o + o / 8] * (sign * a.s[i]));
+            const float x = fmaf(v[i], a.c[i], ex[o + o / 8] * (sign * a.s[i]));
+            v[i] = i < a.live ? x : v[i];
         }
         __syncwarp();
     } else if (p.layout == KDA_ROT_HALF) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float o = __shfl_sync(0xffffffffu, v[i], partner);
-            v[i] = fmaf(v[i], a.c[i], o * (sign * a.s[i]));
+            const float x = fmaf(v[i], a.c[i], o * (sign * a.s[i]));
+            v[i] = a.live > 0 ? x : v[i];  // all of a lane's channels or none
         }
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float x = v[2 * j], y = v[2 * j + 1], s = sign * a.s[j];
-            v[2 * j] = fmaf(x, a.c[j], -y * s);
-            v[2 * j + 1] = fmaf(x, s, y * a.c[j]);
+            v[2 * j] = 2 * j < a.live ? fmaf(x, a.c[j], -y * s) : x;
+            v[2 * j + 1] = 2 * j < a.live ? fmaf(x, s, y * a.c[j]) : y;
         }
     }
 }

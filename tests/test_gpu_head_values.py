@@ -48,3 +48,52 @@ def test_gradient_without_a_norm(d):
     same(g["dq"], np64(dy) * np64(w), "dq")
     with np.errstate(invalid="ignore"):
         same(g["dq_weight"], (np64(dy) * np64(x)).sum((0, 1)), "dq_weight")
+
+
+ANGLES = 50
+HEADS = [  # d, rot, half: one path each
+    (128, 64, True),   # halves of whole lanes
+    (40, 10, True),    # a half inside a lane's channels
+    (128, 60, False),  # neighbouring pairs, the last of them inside a lane's channels
+    (7, 4, True),      # channel by channel
+    (7, 4, False),
+]
+
+
+@pytest.mark.parametrize("d,rot,half", HEADS)
+@pytest.mark.parametrize("norm", ["none", "rms"])
+def test_what_is_not_turned_stays(d, rot, half, norm):
+    """Infinities and NaN in channels past the turned ones, and anywhere in a head whose position is outside the
+    tables, touch no other channel of a head that has no norm, and come out as they are; with a norm they spoil their
+    own head alone."""
+    import kda_recurrent_state_gb300 as kda
+    from kda_recurrent_state_gb300 import binding
+
+    r = rand(d + rot)
+    x, dy, w, ang = r(12, 3, d), r(12, 3, d), r(d), r(ANGLES, rot // 2) * 3
+    cos, sin = ang.cos(), ang.sin()
+    pos = torch.arange(12, device="cuda") * 4
+    pos[3], pos[7] = ANGLES, -1
+    for t in (x, dy):
+        t[0, 0, rot], t[1, 1, rot + 1], t[2, 2, d - 1] = INF, NAN, -INF  # past the turned channels
+        t[3, 0, 0], t[3, 1, rot - 1], t[3, 2, rot // 2] = INF, NAN, -INF  # outside the tables
+        t[7, 1, 1] = NAN
+    kw = dict(norm=kda.KDA_NORM_NONE if norm == "none" else kda.KDA_NORM_RMS, eps=1e-5,
+              layout=kda.KDA_ROT_HALF if half else kda.KDA_ROT_PAIRS)
+    assert kda.kda_get_device_status() == 0
+    out, _ = kda.kda_qk_norm_fwd(x, None, w, None, cos, sin, pos, **kw)
+    g = kda.kda_qk_norm_bwd(x, None, dy, None, w, None, cos, sin, pos, **kw)
+    assert kda.kda_get_device_status() == binding.KDA_STATUS_POSITION_RANGE
+    at = pos.cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        n64 = lambda t: ref.head_fwd(np64(t), np64(w), np64(cos), np64(sin), at, half, norm, 1e-5)
+        turned_back = ref._turn(np64(dy), np64(cos), np64(sin), at, half, back=True)
+        if norm == "none":
+            same(out, n64(x), "out")
+            same(g["dq"], turned_back * np64(w), "dq")
+            same(g["dq_weight"], (turned_back * np64(x)).sum((0, 1)), "dq_weight")
+            return
+        keep = np.isfinite(np64(x)).all(-1)
+        same(out[torch.from_numpy(keep)], n64(x)[keep], "heads without one")
+        want, _ = ref.head_bwd(np64(x), np64(w), np64(cos), np64(sin), at, half, norm, 1e-5, np64(dy))
+        same(g["dq"][torch.from_numpy(keep)], want[keep], "dq of heads without one")
