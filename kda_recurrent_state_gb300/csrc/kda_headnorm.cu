@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(kThreads) head_norm_bwd_kernel(HeadProblem p) 
             }
             ss = head_sum<LPH>(ss);
             hx = head_sum<LPH>(hx);
-            const float inv = inv_norm(p, ss), back = inv * inv * inv * share * hx;
+            // slots past the unit's heads hold zeros, whose 1 / norm without eps is infinite: they add 0, not NaN, to dw
+            const float inv = k < n ? inv_norm(p, ss) : 0.f, back = inv * inv * inv * share * hx;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dw[i] = fmaf(g[i], v[i] * inv, dw[i]);

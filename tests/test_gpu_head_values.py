@@ -97,3 +97,30 @@ def test_what_is_not_turned_stays(d, rot, half, norm):
         same(out[torch.from_numpy(keep)], n64(x)[keep], "heads without one")
         want, _ = ref.head_bwd(np64(x), np64(w), np64(cos), np64(sin), at, half, norm, 1e-5, np64(dy))
         same(g["dq"][torch.from_numpy(keep)], want[keep], "dq of heads without one")
+
+
+NO_EPS = [  # tokens, Hq, Hk, d
+    (5, 3, 1, 64),     # lanes past the last head
+    (3, 1, 1, 40),     # and past the head's channels
+    (8000, 5, 3, 64),  # several heads a unit, the last unit of a token not full
+    (5, 3, 1, 7),      # channel by channel
+]
+
+
+@pytest.mark.parametrize("tokens,Hq,Hk,d", NO_EPS)
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+def test_no_eps(tokens, Hq, Hk, d, norm):
+    """eps = 0: what a launch has beyond its heads adds nothing to the weights' gradients."""
+    import kda_recurrent_state_gb300 as kda
+
+    r = rand(tokens)
+    q, k, wq, wk = r(tokens, Hq, d), r(tokens, Hk, d), r(d), r(d)
+    dq, dk = r(tokens, Hq, d), r(tokens, Hk, d)
+    kw = dict(norm=kda.KDA_NORM_RMS if norm == "rms" else kda.KDA_NORM_L2, eps=0.0)
+    qo, ko = kda.kda_qk_norm_fwd(q, k, wq, wk, **kw)
+    g = kda.kda_qk_norm_bwd(q, k, dq, dk, wq, wk, **kw)
+    for name, x, w, dy, out in (("q", q, wq, dq, qo), ("k", k, wk, dk, ko)):
+        same(out, ref.head_fwd(np64(x), np64(w), None, None, None, True, norm, 0.0), name)
+        dx, dw = ref.head_bwd(np64(x), np64(w), None, None, None, True, norm, 0.0, np64(dy))
+        same(g["d" + name], dx, "d" + name)
+        same(g[f"d{name}_weight"], dw, f"d{name}_weight")
