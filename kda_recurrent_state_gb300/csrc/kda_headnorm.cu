@@ -5,7 +5,8 @@
 //   y = n with its first `rot` entries turned in pairs (a, b) by the angle of (m, pair):
 //       (a cos - b sin, a sin + b cos), pairs (i, i + rot/2) or (2i, 2i + 1).
 // Backwards, with g = dy turned back:  dw = sum g r x,   h = g w,
-//   dx = r h - x r^3 s <h, x>,   s = 1/d (RMS), 1 (L2);   dx = h (none: x has no part in it).
+//   dx = r (h - u s <h, u>),  u = r x,   s = 1/d (RMS), 1 (L2);   dx = h (none: x has no part in it)
+// (r^3 is never formed: it overflows from norms of 1e-13 down).
 //
 // Bound by HBM: each head is read once and written once.  A head is held by a power of two of
 // lanes, 8 channels each (16 bytes of bf16, 32 of fp32), so its sums are shuffles and the half
@@ -298,11 +299,12 @@ __global__ void __launch_bounds__(kThreads) head_norm_bwd_kernel(HeadProblem p) 
             ss = head_sum<LPH>(ss);
             hx = head_sum<LPH>(hx);
             // slots past the unit's heads hold zeros, whose 1 / norm without eps is infinite: they add 0, not NaN, to dw
-            const float inv = k < n ? inv_norm(p, ss) : 0.f, back = inv * inv * inv * share * hx;
+            const float inv = k < n ? inv_norm(p, ss) : 0.f, along = share * (inv * hx);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                dw[i] = fmaf(g[i], v[i] * inv, dw[i]);
-                v[i] = p.norm == KDA_NORM_NONE ? gw[i] : fmaf(gw[i], inv, -v[i] * back);
+                const float unit = v[i] * inv;
+                dw[i] = fmaf(g[i], unit, dw[i]);
+                v[i] = p.norm == KDA_NORM_NONE ? gw[i] : inv * fmaf(-along, unit, gw[i]);
             }
             if (mine && k < n) st_vec<8>(dx + k * p.d, v);
         }
@@ -402,19 +404,19 @@ __global__ void __launch_bounds__(kThreads) head_norm_any_kernel(HeadProblem p) 
                 g[i] = 0.f;
                 if (e < p.d) {
                     const float t = turned(p, sv, e, row, -1.f);
-                    const float n = t * v[i] * inv;
+                    const float n = t * (v[i] * inv);
                     if (which) dw[1][i] += n;
                     else dw[0][i] += n;
                     g[i] = t * (p.weight[which] ? __ldg(p.weight[which] + e) : 1.f);
                 }
                 hx = fmaf(g[i], v[i], hx);
             }
-            const float back = inv * inv * inv * grad_share(p) * head_sum<32>(hx);
+            const float along = grad_share(p) * (inv * head_sum<32>(hx));
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
                 const int e = lane + 32 * i;
                 if (e < p.d) {
-                    float f[1] = {fmaf(g[i], inv, -v[i] * back)};
+                    float f[1] = {inv * fmaf(-along, v[i] * inv, g[i])};
                     // one channel: h and x are parallel, and 1 - x^2 r^2 = eps r^2 takes the place of the difference
                     if (p.d == 1) f[0] = g[i] * inv * (p.eps * inv * inv);
                     if (p.norm == KDA_NORM_NONE) f[0] = g[i];

@@ -124,3 +124,29 @@ def test_no_eps(tokens, Hq, Hk, d, norm):
         dx, dw = ref.head_bwd(np64(x), np64(w), None, None, None, True, norm, 0.0, np64(dy))
         same(g["d" + name], dx, "d" + name)
         same(g[f"d{name}_weight"], dw, f"d{name}_weight")
+
+
+FAR = [(d, scale, eps) for d in (128, 40, 7, 1)
+       for scale, eps in ((2.0 ** -50, 0.0), (2.0 ** -50, 2.0 ** -98), (2.0 ** 40, 1e-6))
+       if d > 1 or scale < 1]  # one large channel: eps r^3 is below fp32's smallest ordinary number
+
+
+@pytest.mark.parametrize("d,scale,eps", FAR)
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+def test_norms_far_from_one(d, scale, eps, norm):
+    """Heads whose norm is far from 1 (its square is still an ordinary fp32 number, its cube's inverse is not): the
+    gradients are those of the definition.  One channel without eps has no gradient: exactly 0."""
+    import kda_recurrent_state_gb300 as kda
+
+    r = rand(d)
+    x, w, dy = (1 + r(30, 3, d).abs()) * scale, r(d), r(30, 3, d)
+    kw = dict(norm=kda.KDA_NORM_RMS if norm == "rms" else kda.KDA_NORM_L2, eps=eps)
+    out, _ = kda.kda_qk_norm_fwd(x, None, w, **kw)
+    g = kda.kda_qk_norm_bwd(x, None, dy, None, w, **kw)
+    same(out, ref.head_fwd(np64(x), np64(w), None, None, None, True, norm, eps), "out")
+    dx, dw = ref.head_bwd(np64(x), np64(w), None, None, None, True, norm, eps, np64(dy))
+    if d == 1:  # r h - x r^3 <h, x> is eps r^3 h: the definition's own difference cancels even in 64 bits
+        m = np64(x) ** 2 + eps
+        dx = np64(dy) * np64(w) * eps * m ** -1.5
+    same(g["dq"], dx, "dq")
+    same(g["dq_weight"], dw, "dq_weight")
