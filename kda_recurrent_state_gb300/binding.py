@@ -120,7 +120,16 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _same_device(dev: int, what: str) -> None:
+    """The library launches on the current device: the tensors, and with them the stream, must be that one's."""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{what} cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}: "
+                         "call under torch.cuda.device")
+
+
 def _stream(device) -> ctypes.c_void_p:
+    if device is not None and device.index is not None:
+        _same_device(device.index, "the tensors are on")
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
@@ -470,6 +479,7 @@ def _on_gpu(t, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    _same_device(dev, f"{name} is on")
     return dev
 
 
