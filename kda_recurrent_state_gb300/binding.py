@@ -485,7 +485,7 @@ def _on_gpu(t, name: str) -> int:
 
 # The handle of a device's current stream; the plain accessor builds a Stream object around it each time.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_raw_stream(dev).cuda_stream)
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _sequences(lead, cu_seqlens, dev: int):

@@ -34,3 +34,17 @@ def test_streams_of_another_device_are_refused(monkeypatch):
         binding._stream(torch.device("cuda:1"))
     for device in (torch.device("cuda:0"), torch.device("cuda"), None):
         assert binding._stream(device).value == 5
+
+
+def test_stream_handle_without_the_raw_accessor(monkeypatch):
+    """Where torch lacks the accessor of the bare handle, the handle comes from the Stream object."""
+    class Stream:
+        def __init__(self, device):
+            self.cuda_stream = 40 + device
+
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    spec = importlib.util.spec_from_file_location("binding_without_accessor", binding.__file__)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    assert module._raw_stream(2) == 42
