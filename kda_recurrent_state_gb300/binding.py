@@ -670,8 +670,8 @@ def _head_args(q, k, q_weight, k_weight, cos, sin, positions, dev):
     f32 = torch.float32
     weights = [_full(q_weight, "q_weight", (d,), f32, dev), _full(k_weight, "k_weight", (d,), f32, dev)]
     rot, tables = 0, [None, None, None, 0]
-    if cos is not None:
-        if sin is None or positions is None or cos.dim() != 2:
+    if cos is not None or sin is not None:  # positions alone turn nothing
+        if cos is None or sin is None or positions is None or cos.dim() != 2:
             raise ValueError("the rotation wants cos and sin [positions, rot / 2] and positions")
         rot = 2 * cos.shape[1]
         tables = [_full(cos, "cos", cos.shape, f32, dev), _full(sin, "sin", cos.shape, f32, dev),
