@@ -120,7 +120,8 @@ __device__ __forceinline__ void load_angles(const HeadProblem& p, int64_t row, i
     }
 }
 // v turned (sign = 1) or turned back (sign = -1).  `partner`: the lane that holds the other half;
-// `ex`: the group's shared memory, 9 floats a lane (an odd distance keeps the banks apart).
+// `ex`: the group's shared memory, 9 floats a lane (an odd distance keeps the banks apart), the ninth 0: the
+// partner of a channel that is not turned.
 template <bool kMixed>
 __device__ __forceinline__ void turn(const HeadProblem& p, const Angles& a, float sign, int partner, int e0, float* ex,
                                      float (&v)[8]) {
@@ -129,12 +130,12 @@ __device__ __forceinline__ void turn(const HeadProblem& p, const Angles& a, floa
         const int half = p.rot / 2;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ex[e0 + e0 / 8 + i] = v[i];
+        ex[e0 + e0 / 8 + 8] = 0.f;
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int e = e0 + i, o = e < half ? e + half : e < p.rot ? e - half : e;
-            const float x = fmaf(v[i], a.c[i], ex[o + o / 8] * (sign * a.s[i]));
-            v[i] = i < a.live ? x : v[i];
+            const int e = e0 + i, o = e < half ? e + half : e - half;
+            v[i] = fmaf(v[i], a.c[i], ex[i < a.live ? o + o / 8 : e0 + e0 / 8 + 8] * (sign * a.s[i]));
         }
         __syncwarp();
     } else if (p.layout == KDA_ROT_HALF) {
@@ -236,8 +237,9 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(HeadProblem p) {
 
 // Gradients: the first `q_blocks` blocks take the queries' units, the rest the keys', each with its
 // share's stride, so that a thread has one set of weights and of sums of dw.  A block adds its groups'
-// sums in order and writes one row of `partial`.
-template <typename T, typename Tg, int LPH, bool kMixed>
+// sums in order and writes one row of `partial`.  kNorm: there is a norm (a variant without one, because a test at
+// every value cost 8 us of 218 at 32,768 x 40 heads of 128 channels).
+template <typename T, typename Tg, int LPH, bool kMixed, bool kNorm>
 __global__ void __launch_bounds__(kThreads) head_norm_bwd_kernel(HeadProblem p) {
     __shared__ float s_dw[kThreads / LPH][LPH * 8];
     __shared__ float s_ex[kMixed ? kThreads * 9 : 1];
@@ -296,15 +298,23 @@ __global__ void __launch_bounds__(kThreads) head_norm_bwd_kernel(HeadProblem p) 
                 ss = fmaf(v[i], v[i], ss);
                 hx = fmaf(gw[i], v[i], hx);
             }
-            ss = head_sum<LPH>(ss);
-            hx = head_sum<LPH>(hx);
-            // slots past the unit's heads hold zeros, whose 1 / norm without eps is infinite: they add 0, not NaN, to dw
-            const float inv = k < n ? inv_norm(p, ss) : 0.f, along = share * (inv * hx);
+            if constexpr (kNorm) {
+                ss = head_sum<LPH>(ss);
+                hx = head_sum<LPH>(hx);
+                // slots past the unit's heads hold zeros, whose 1 / norm without eps is infinite: they add 0, not NaN, to dw
+                const float inv = k < n ? inv_norm(p, ss) : 0.f, along = share * (inv * hx);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float unit = v[i] * inv;
-                dw[i] = fmaf(g[i], unit, dw[i]);
-                v[i] = p.norm == KDA_NORM_NONE ? gw[i] : inv * fmaf(-along, unit, gw[i]);
+                for (int i = 0; i < 8; ++i) {
+                    const float unit = v[i] * inv;
+                    dw[i] = fmaf(g[i], unit, dw[i]);
+                    v[i] = inv * fmaf(-along, unit, gw[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dw[i] = fmaf(g[i], v[i], dw[i]);
+                    v[i] = gw[i];
+                }
             }
             if (mine && k < n) st_vec<8>(dx + k * p.d, v);
         }
@@ -476,8 +486,9 @@ bool vector_ok(const HeadProblem& p) {
 
 template <typename T, typename To, bool kBwd, int LPH, bool kMixed>
 cudaError_t run_mixed(const HeadProblem& p, int64_t grid, cudaStream_t st) {
-    if constexpr (kBwd) head_norm_bwd_kernel<T, To, LPH, kMixed><<<(unsigned)grid, kThreads, 0, st>>>(p);
-    else head_norm_kernel<T, To, LPH, kMixed><<<(unsigned)grid, kThreads, 0, st>>>(p);
+    if constexpr (!kBwd) head_norm_kernel<T, To, LPH, kMixed><<<(unsigned)grid, kThreads, 0, st>>>(p);
+    else if (p.norm != KDA_NORM_NONE) head_norm_bwd_kernel<T, To, LPH, kMixed, true><<<(unsigned)grid, kThreads, 0, st>>>(p);
+    else head_norm_bwd_kernel<T, To, LPH, kMixed, false><<<(unsigned)grid, kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
 template <typename T, typename To, bool kBwd, int LPH>
