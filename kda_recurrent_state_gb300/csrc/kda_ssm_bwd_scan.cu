@@ -31,9 +31,9 @@ cudaError_t launch_ssm_bwd_scans(const BwdArgs& b, int in_dtype, int grad_dtype,
         q.seg_dt = b.seg_dt;
         q.seg_grad = b.seg_g;
     }
-    const int cw = 64 / scan_lanes(b.p.N), step = cw < 8 ? 8 / cw : 1, per_group = b.p.D / b.p.G;
+    const int cw = 64 / scan_lanes(b.p.N), per_group = b.p.D / b.p.G;
     q.scan_warps = kMostScan;
-    while (q.scan_warps > step && (q.scan_warps - step) * cw >= per_group) q.scan_warps -= step;
+    while (q.scan_warps > 1 && (q.scan_warps - 1) * cw >= per_group) --q.scan_warps;
     if (in_dtype == KDA_BF16)
         return grad_dtype == KDA_BF16 ? run<__nv_bfloat16, __nv_bfloat16>(q, st) : run<__nv_bfloat16, float>(q, st);
     return grad_dtype == KDA_BF16 ? run<float, __nv_bfloat16>(q, st) : run<float, float>(q, st);

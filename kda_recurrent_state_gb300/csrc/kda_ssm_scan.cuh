@@ -427,16 +427,16 @@ struct ScanPlan {
     int64_t len;
 };
 inline ScanPlan scan_plan(int64_t seqs, int64_t T_total, int64_t T_uniform, int D, int G, int N, bool packed) {
-    const int cw = 64 / scan_lanes(N), per_group = D / G, step = cw < 8 ? 8 / cw : 1;  // groups of 8 channels
+    const int cw = 64 / scan_lanes(N), per_group = D / G;  // cw: whole groups of 8 channels
     auto blocks = [&](int w) { return (int64_t)G * ((per_group + w * cw - 1) / (w * cw)); };
     int most = kMostScan;
-    while (most > step && (most - step) * cw >= per_group) most -= step;
+    while (most > 1 && (most - 1) * cw >= per_group) --most;
     if (!packed && seqs * blocks(most) >= 96) {
         // Whole sequences fill the chip: of 3 or 4 scan warps the number whose CTAs, one an SM, fill
         // their last wave best (fewer warps would leave an SM's pipes idle).
         int best = most;
         int64_t cost = INT64_MAX;
-        for (int w = most; w > most / 2; w -= step) {
+        for (int w = most; w > most / 2; --w) {
             const int64_t c = (seqs * blocks(w) + 151) / 152 * w;
             if (c < cost) {
                 cost = c;
