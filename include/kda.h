@@ -448,7 +448,11 @@ int kda_ssm_step(const void* u, int64_t u_stride, const void* delta, int64_t del
  *   du, ddelta, dz [.., D] grad_dtype (dz with z, else NULL)
  *   dA [D, n_state], dB, dC [.., G, n_state], dskip [D] (or NULL), ddelta_bias [D] (or NULL),
  *   d_init [N, D, n_state] (or NULL) float32
- *   workspace kda_ssm_bwd_workspace_size bytes, 16-byte aligned.
+ *   workspace kda_ssm_bwd_workspace_size bytes, 16-byte aligned.  Most of it, in bytes a token: the kept
+ *             states, 4 D for n_state <= 16, 8 D up to 32, 16 D up to 64; and partial dB, dC, 8 G n_state
+ *             for every block of a group's channels (of at most 2048 / n_state channels, n_state rounded up to
+ *             a power of two of at least 4).  4 sequences of 2048 tokens: 21 KB a token for
+ *             D = 4096, n_state = 16, and 307 KB for D = 8192, n_state = 64.
  * The states are recomputed from the inputs.  Sums run in a fixed order: results are reproducible.
  */
 int kda_ssm_bwd(const void* u, int64_t u_stride, const void* delta, int64_t delta_stride, const float* A, const void* B,

@@ -526,8 +526,8 @@ def kda_conv_fwd(x, weight, bias=None, init_state=None, out=None, final_state=No
                  activation: int = KDA_ACT_SILU, out_dtype=None, return_final_state: bool = True):
     """Short causal convolution over each channel.  x [B,T,D], or [Ttot,D] with cu_seqlens (int64 [N+1]); a slice
     of a wider tensor's last dimension is read in place.  weight [D,W] fp32 (W = 2, 3, 4), bias [D] fp32 or None,
-    init_state [N,W-1,D] in x's dtype or None (zeros).  Returns (out, final_state); out in out_dtype (x's dtype
-    by default).  final_state may be init_state itself."""
+    init_state [N,W-1,D] in x's dtype or None (zeros).  Returns (out, final_state); a new out has out_dtype
+    (x's dtype by default), a given one keeps its own.  final_state may be init_state itself."""
     dev, lead = _on_gpu(x, "x"), x.shape[:-1]
     cu, N, T, _ = _sequences(lead, cu_seqlens, dev)
     D, W, xs, w, b = _conv_args(x, weight, bias, lead, dev)
@@ -598,8 +598,8 @@ def kda_ssm_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, init_state=N
                 workspace=None):
     """Selective state space scan.  u, delta (and the gate z) [B,T,D], or [Ttot,D] with cu_seqlens; B, C [..,G,n]
     with G dividing D, all in u's dtype, slices of wider tensors read in place; A [D,n] fp32 (n <= 64), D and
-    delta_bias [D] fp32 or None, init_state [N,D,n] fp32 or None.  Returns (out, final_state [N,D,n] fp32); out in
-    out_dtype (u's dtype by default)."""
+    delta_bias [D] fp32 or None, init_state [N,D,n] fp32 or None.  Returns (out, final_state [N,D,n] fp32); a new out
+    has out_dtype (u's dtype by default), a given one keeps its own."""
     dev, lead = _on_gpu(u, "u"), u.shape[:-1]
     cu, N, T, total = _sequences(lead, cu_seqlens, dev)
     head, (Dm, n, G) = _ssm_args(u, delta, A, B, C, D, z, delta_bias, delta_softplus, lead, dev)
@@ -684,8 +684,8 @@ def kda_qk_norm_fwd(q, k=None, q_weight=None, k_weight=None, cos=None, sin=None,
                     out_dtype=None):
     """Norm of every query and key head with the position rotation in the same pass.  q [..,Hq,d], k [..,Hk,d] or
     None (slices of wider tensors are read in place), weights [d] fp32 or None; cos, sin [P, rot/2] fp32 and
-    positions [..] int64 turn the first rot channels (None: no rotation).  Returns (q_out, k_out) in out_dtype (q's
-    dtype by default)."""
+    positions [..] int64 turn the first rot channels (cos and sin None: no rotation, whatever the positions).  Returns
+    (q_out, k_out); new ones have out_dtype (q's dtype by default), given ones share a dtype."""
     dev = _on_gpu(q, "q")
     (lead, tokens, Hq, Hk, d, rot), ptrs, weights, tables = _head_args(q, k, q_weight, k_weight, cos, sin, positions, dev)
     if q_out is None:

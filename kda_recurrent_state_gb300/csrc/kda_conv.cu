@@ -13,8 +13,12 @@
 //
 // Measured (GB300, bf16, W = 4, SiLU): 188,232 tokens x 8192 channels 1.005 ms, 6.14 TB/s, 0.92 of the
 // copy rate; gradients of 32,768 x 4096 0.193 ms, 4.2 TB/s, 0.62 of it: 20 operations an element and
-// 128 registers a thread (sums, weights and windows of 4 channels) leave 16 warps an SM, too few to
-// hide all of the loads; 8 channels a thread, 5 CTAs an SM or longer batches were slower.
+// 128 registers a thread, which leave 16 warps an SM and do not hold the sums, weights and windows of 4
+// channels beside a batch of rows: the variants of 4 channels spill (bytes of spill stores a thread for 4, 3
+// and 2 taps: x and gradients bf16 156, 104, 48; bf16 and fp32 504, 252, 156; fp32 and bf16 396, 320, 200;
+// fp32 1192, 536, 696).  That size with 4 taps: bf16 x with fp32 gradients 0.256 ms (bytes alone 0.201), fp32
+// with bf16 0.238 (0.161), fp32 0.557 (0.241).  In bf16 8 channels a thread, 5 CTAs an SM and longer batches were
+// slower, and 4 rows a batch too (0.208 against 0.199 then); the choice was not timed in the other types.
 #include <type_traits>
 
 #include "kda_vec.cuh"
@@ -168,7 +172,9 @@ __global__ void __launch_bounds__(kThreads, 4) conv_fwd_kernel(ConvProblem p) {
     }
 }
 
-// One token per session, the state moved on in place.  A thread takes L sessions of its channels.
+// One token per session, the state moved on in place.  A thread takes L sessions of its channels, two at a
+// time: the next two are loaded into the registers of the last ones, so their latency is waited for.  256 sessions
+// of 12,288 channels: four such rounds at 10 warps an SM, 13 us with cold inputs against 7.6 for the bytes.
 template <typename T, typename To, int V, int W>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvProblem p) {
     constexpr int kSess = 2;  // in flight

@@ -15,9 +15,10 @@
 // a token, whose loads are issued together.  Sizes or alignments that do not allow vectors of 8
 // take one warp per head, channel by channel.
 //
-// Measured (GB300, bf16, d = 128): unit length of 32,768 x 192 heads 0.476 ms, 6.77 TB/s, the copy
-// rate; gradients of a weighted norm with 64 turned channels, 32,768 x 40 heads, 0.208 ms, 4.9 TB/s,
-// 0.73 of it (two sums over the head, eight shuffles and 16 warps an SM: issue 58 % busy).
+// Measured (GB300, bf16, d = 128): unit length of 32,768 x 192 heads 0.478 ms, 6.74 TB/s, the copy
+// rate; gradients of a weighted norm with 64 turned channels, 32,768 x 40 heads, 0.210 ms, 4.8 TB/s,
+// 0.72 of it: the loads of 16 warps an SM (107 registers) and the sums over a head's lanes are waited for, no
+// unit is at its limit (issue 58 % busy).
 #include "kda_vec.cuh"
 
 namespace kda {

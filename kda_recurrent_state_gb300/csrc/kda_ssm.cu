@@ -3,8 +3,9 @@
 //   dt = softplus(delta_t + bias) (or delta_t + bias)      a = exp(dt A)
 //   h_t = a h_{t-1} + dt u_t B_t        y_t = <C_t, h_t> + skip u_t        out_t = y_t z_t sigmoid(z_t).
 //
-// Work per (token, channel): N exponentials and 4 N fp32 operations against 6 to 8 bytes of bf16,
-// so for N = 16 the exponential and fp32 units are the bound, a little above the time of the bytes.
+// Work per (token, channel): N exponentials and 4 N fp32 operations against 6 to 8 bytes of bf16: for
+// N = 16 the fp32 units need 1.7 times the time of the bytes, and the scan takes 2.6 times theirs
+// (kda_ssm_scan.cuh says why).
 //
 // Prompt: the scan of kda_ssm_scan.cuh, a CTA per (sequence, block of channels).
 // With too few (sequence, channel) pairs to fill the chip the token axis is cut into segments:

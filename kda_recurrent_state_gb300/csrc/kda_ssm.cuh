@@ -47,7 +47,9 @@ __device__ __forceinline__ f2 dup(float a) { return f2{a, a}; }
 // exp(dt A) with A already times log2 e.  The hardware's 2^x lies on average 0.2 .. 0.9 x 2^-25 below
 // the true value for x in [-0.25, 0] (measured, 2^20 points an octave), and a recurrence raises its
 // decay to the power of its memory: the exponent is moved up by 0.5 x 2^-25 / ln 2, which takes the
-// middle of that bias away where the memory is long (for large |x| it is below the rounding).
+// middle of that bias away where the memory is long (for large |x| it is below the rounding; an exponent of
+// 0 still gives exactly 1).  It makes the product dt A a fused operation; times with and without it are the
+// same (4 x 8192 x 4096 forward 732 us, 4 x 2048 x 4096 gradients 979 to 983 us, N = 16).
 constexpr float kNudge = 2.2e-8f;
 __device__ __forceinline__ f2 decay2(f2 dt, f2 A) { return ex2_2(fma2(dt, A, dup(kNudge))); }
 __device__ __forceinline__ float decay1(float dt, float A) { return ex2(fmaf(dt, A, kNudge)); }

@@ -15,13 +15,14 @@
 //      state every 4 tokens in shared memory; each group of 4 tokens is then recomputed once more
 //      with a and a h_{t-1} in registers and undone in reverse order;
 //   4. sums over segments (dA, dskip, dbias) and over channel blocks (dB, dC) in a fixed order.
-// Bound by the issue of fp32 work and shuffles, not by the bytes: 3 exponentials and about 20 fp32
+// The time goes into fp32 work and shuffles, not into the bytes: 3 exponentials and about 20 fp32
 // operations per (token, channel, state), which alone take 0.32 ms at 4 x 2048 x 4096, N = 16 (the bytes:
 // 0.08 ms).  A thread holds 2 channels x 4 states in (3); the next chunk's rows come by background
 // copies while a chunk is worked on.
 //
 // Measured there: 0.98 ms, of it 0.17 in (1) and 0.80 in (3) (issue 48 %, fp32 38 %, shared memory 55 %
-// busy; 7 warps an SM at 229 registers).  A group's results are stored after all of its tokens: with a
+// busy; 7 warps an SM at 229 registers, so latency is exposed, and the phases of a chunk stand between
+// barriers).  A group's results are stored after all of its tokens: with a
 // store between, the next token's loads waited, and (3) took 0.94 ms.  CTAs of 4 warps, two an SM, cost the
 // same (their units do not divide over the SMs), and so did one CTA as two halves with their own
 // barriers (0.99 ms); groups of 2 tokens would double the kept states.

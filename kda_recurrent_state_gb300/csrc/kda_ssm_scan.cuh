@@ -6,10 +6,12 @@
 // while its scan warps, with 2 channels x 8 states a thread in registers, run the tile between: the
 // scan's chains of fp32 and exponential work are not interrupted by loads, softplus or the gate.
 //
-// Bound by the issue of fp32 work: per (token, 32 channels x 16 states) 64 fp32 operations on register
-// pairs, each occupying the operand ports for 2 (product) to 3 (fused) cycles, and 64 cycles of
-// exponentials beside them: about 120 cycles of a scheduler, and 45 for the helpers' work, where
-// 4 x 8192 x 4096 takes 170 (0.73 ms on the 128 SMs that its 128-channel blocks fill).
+// What bounds it: per (token, 32 channels x 16 states) 32 fp32 operations on register pairs, each occupying
+// the operand ports for 2 (product) to 3 (fused, three different operands) cycles, about 80 cycles of a
+// scheduler, and beside them 16 exponentials, 64 cycles of their unit.  4 x 8192 x 4096 takes 170 cycles
+// and 104 instructions (0.73 ms on the 128 SMs that its 128-channel blocks fill): issue 56 %, fp32 pipes
+// 50 % with the helpers' work, exponentials 39 %.  No unit is at its limit; one scan warp and one helper warp
+// a scheduler leave the latency of their chains exposed.
 //
 // Tried and slower: 1 channel x 8 states a thread on 148 SMs (0.77 ms: twice the loads of B and C);
 // 8 helper warps (0.82: they take issue slots from the scan); the next token's decays computed ahead
