@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(ScanArgs q) {
     seq_range(p.seqs, s, a, e);
     const int64_t count = e > a ? (e - a + q.g.len - 1) / q.g.len : 1;
     if (count == 1) return;
-    const float A = kLog2e * p.A[o];
+    const float A = log2_rate(p.A[o]);
     float h = p.init ? p.init[i] : 0.f;
     const int64_t first = slot_of(q.g, s, 0);
     float* st = q.seg_state + first * per + o;
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs q, unsigned gx)
     }
     float A[4];
 #pragma unroll
-    for (int n = 0; n < 4; ++n) A[n] = n0 + n < p.N ? kLog2e * __ldg(p.A + (int64_t)c * p.N + n0 + n) : 0.f;
+    for (int n = 0; n < 4; ++n) A[n] = n0 + n < p.N ? log2_rate(__ldg(p.A + (int64_t)c * p.N + n0 + n)) : 0.f;
     const float bias = p.bias ? __ldg(p.bias + c) : 0.f, skip = p.skip ? __ldg(p.skip + c) : 0.f;
     float dt[OWN], u[OWN], y[SESS];
 #pragma unroll

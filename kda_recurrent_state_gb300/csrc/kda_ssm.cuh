@@ -7,6 +7,8 @@
 // they stay zero and add zero.
 #pragma once
 
+#include <cfloat>
+
 #include "kda_vec.cuh"
 
 namespace kda {
@@ -51,6 +53,11 @@ __device__ __forceinline__ f2 dup(float a) { return f2{a, a}; }
 // 0 still gives exactly 1).  It makes the product dt A a fused operation; times with and without it are the
 // same (4 x 8192 x 4096 forward 732 us, 4 x 2048 x 4096 gradients 979 to 983 us, N = 16).
 constexpr float kNudge = 2.2e-8f;
+// A times log2 e, finite where A is: a step of 0 times an infinite rate would be NaN where exp(0 A) is 1.
+__device__ __forceinline__ float log2_rate(float A) {
+    const float r = kLog2e * A;
+    return isinf(r) && !isinf(A) ? copysignf(FLT_MAX, A) : r;
+}
 __device__ __forceinline__ f2 decay2(f2 dt, f2 A) { return ex2_2(fma2(dt, A, dup(kNudge))); }
 __device__ __forceinline__ float decay1(float dt, float A) { return ex2(fmaf(dt, A, kNudge)); }
 

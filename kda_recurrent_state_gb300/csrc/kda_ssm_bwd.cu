@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(256) ssm_bwd_carry_kernel(BwdArgs q) {
     int64_t a, e;
     seq_range(p.seqs, s, a, e);
     const int64_t count = e > a ? (e - a + q.g.len - 1) / q.g.len : 1;
-    const float A = kLog2e * p.A[o];
+    const float A = log2_rate(p.A[o]);
     const int64_t first = slot_of(q.g, s, 0);
     float* sh = q.seg_h + first * per + o;
     float* sg = q.seg_g + first * per + o;
@@ -163,8 +163,7 @@ __global__ void __launch_bounds__(32 * kMostWarps, 1) ssm_bwd_kernel(BwdArgs q) 
     gather(p.A, A);
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-        A[n].x *= kLog2e;
-        A[n].y *= kLog2e;
+        A[n] = f2{log2_rate(A[n].x), log2_rate(A[n].y)};
         dA[n] = dup(0.f);
         h0[n] = dup(0.f);
         dh[n] = dup(0.f);

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(32 * (kMostScan + kHelpWarps), 1) scan_kernel(
                     const int st = 8 * ln + 2 * n + m;
                     const bool in = c0 + k < cend && st < p.N;
                     const int64_t o = (int64_t)(c0 + k) * p.N + st;
-                    av[m] = in ? kLog2e * __ldg(p.A + o) : 0.f;
+                    av[m] = in ? log2_rate(__ldg(p.A + o)) : 0.f;
                     hv[m] = 0.f;
                     if (kMain && in && q.seg_state && seg.count > 1) hv[m] = q.seg_state[slot * p.D * p.N + o];
                     else if ((kMain || (kMode == Scan::kKeep && seg.i == 0)) && in && p.init)
