@@ -7,8 +7,6 @@
 // they stay zero and add zero.
 #pragma once
 
-#include <cfloat>
-
 #include "kda_vec.cuh"
 
 namespace kda {
@@ -54,9 +52,10 @@ __device__ __forceinline__ f2 dup(float a) { return f2{a, a}; }
 // same (4 x 8192 x 4096 forward 732 us, 4 x 2048 x 4096 gradients 979 to 983 us, N = 16).
 constexpr float kNudge = 2.2e-8f;
 // A times log2 e, finite where A is: a step of 0 times an infinite rate would be NaN where exp(0 A) is 1.
+// Rates beyond 2.36e38 are taken as they are: any step but 0 (or one below 1e-36) forgets everything.
 __device__ __forceinline__ float log2_rate(float A) {
     const float r = kLog2e * A;
-    return isinf(r) && !isinf(A) ? copysignf(FLT_MAX, A) : r;
+    return isinf(r) ? A : r;
 }
 __device__ __forceinline__ f2 decay2(f2 dt, f2 A) { return ex2_2(fma2(dt, A, dup(kNudge))); }
 __device__ __forceinline__ float decay1(float dt, float A) { return ex2(fmaf(dt, A, kNudge)); }
